@@ -213,7 +213,11 @@ class SharedDecoder:
     def decode(self, cfg, st: LayerState, prefix_table: torch.Tensor, q: torch.Tensor,
                softmax_scale: float, out=None, stream=None) -> torch.Tensor:
         """xmla_decode_shared on raw q (cfg None: q_pe is rotated already);
-        st.seqlens are whole lengths, st.block_table is indexed by logical page."""
+        st.seqlens are whole lengths, st.block_table is indexed by logical page.
+        st's cache is the bf16 one (a page of the 8-bit pool is about half as long:
+        read as bf16 rows it would end outside the pool)."""
+        if st.cache != "bf16":
+            raise ValueError("the shared-prefix decode reads a bf16 cache (read_back_q8 makes one)")
         out = self.out if out is None else out
         xmla.xmla_decode_shared(cfg, q, st.W_UK, st.W_UV, st.pool, st.num_blocks, prefix_table,
                                 self.prefix_pages, st.block_table, st.max_blocks, st.seqlens,
@@ -264,6 +268,8 @@ def append_normed_rows(cfg, st: LayerState, kv: torch.Tensor, kv_weight: torch.T
 def read_back_q8(st: LayerState, seqlens: list[int], status=None, stream=None) -> LayerState:
     """The sequences of an 8-bit cache (their first seqlens[b] tokens) as a bf16 cache
     of consecutive pages, on which any xmla_decode call on `stream` runs."""
+    if st.cache != "q8":
+        raise ValueError("the rows of an 8-bit cache are read back; this one is bf16 already")
     dev = st.pool.device
     pages = [(n + PAGE - 1) // PAGE for n in seqlens]
     first = [sum(pages[:b]) for b in range(len(pages))]
