@@ -228,7 +228,8 @@ int32_t xmla_decode_num_splits(int32_t batch, int32_t q_len, int64_t max_seqlen,
  *                   the q_len newest tokens, which are in the cache already)
  *   out[b,j,h]    = W_UV[h]^T (sum_t P c_kv[t])                  (128)
  * Tokens are read in logical order through block_table (token t of sequence b
- * is row t % 64 of block block_table[b*max_blocks + t/64]).
+ * is row t % 64 of block block_table[b*max_blocks + t/64]).  A NaN in a row that
+ * a query sees makes its output NaN.
  *   cfg: YaRN parameters used to rotate q_pe (host pointer);
  *   q: device bf16 [batch, q_len, 32, 192] = [q_nope 128 | q_pe 64], q_pe NOT
  *      rotated (the call rotates it).  This deliberately differs from
@@ -451,10 +452,10 @@ size_t xmla_decode_shared_workspace_size(int32_t batch, int32_t q_len, int32_t p
  * in fp16 with fp32 accumulation: cache values and absorbed queries
  * (softmax_scale * log2(e) * W_UK^T q_nope) must stay below 65504 in magnitude;
  * a larger one becomes infinite.  Those below 2^-14 are held to 2^-25, so that a
- * cache of values below about 2^-16 loses accuracy.  A NaN or infinity in a token's row spoils the
- * outputs of the sequences that hold the token, and no others.  With up to four
- * queries in all (batch * q_len) the call attends each sequence whole, like
- * xmla_decode.
+ * cache of values below about 2^-16 loses accuracy.  A NaN in a token's row, or
+ * an infinity in its latent, makes the outputs of the sequences that hold the
+ * token NaN, and no others.  With up to four queries in all (batch * q_len) the
+ * call attends each sequence whole, like xmla_decode.
  * Supported: 1 <= batch, 1 <= q_len <= 8, 1 <= prefix_pages, batch * q_len *
  * 64 < 2^31, other limits as in xmla_decode.  Errors: XMLA_ERR_INVALID_ARG,
  * XMLA_ERR_SHAPE, XMLA_ERR_WORKSPACE, XMLA_ERR_CUDA, XMLA_ERR_UNSUPPORTED;

@@ -552,8 +552,10 @@ __device__ __forceinline__ void fma4(float4& acc, float w, const float4& x) {
 // together and merged against the group's maximum over its first 16 splits
 // (lane k of the 16-lane group loads (m, l) of the group's k-th split); later
 // splits are loaded one by one and merged online.  Splits with l = 0 (no
-// token) are skipped.  po / pml: the row's O slice and (m, l) of split 0;
-// splits are o_stride floats and ml_stride (m, l) pairs apart.
+// token) are skipped, and only those: the sum of a split with a NaN or an
+// infinity among its tokens is NaN and has to reach the output.  po / pml: the
+// row's O slice and (m, l) of split 0; splits are o_stride floats and ml_stride
+// (m, l) pairs apart.
 __device__ __forceinline__ void merge_group(const float* po, const float2* pml, int64_t o_stride,
                                             int64_t ml_stride, int nsplit, int sub, int gpr, int q4,
                                             bool active, float& m_g, float& l_g, float4& acc) {
@@ -569,7 +571,7 @@ __device__ __forceinline__ void merge_group(const float* po, const float2* pml, 
                                               : make_float2(-INFINITY, 0.f);
 
   // group maximum over its first 16 splits (lanes of one group: 16 consecutive)
-  m_g = ml.y > 0.f ? ml.x : -INFINITY;
+  m_g = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m_g = fmaxf(m_g, __shfl_xor_sync(0xffffffffu, m_g, o));
   l_g = 0.f;
@@ -578,7 +580,7 @@ __device__ __forceinline__ void merge_group(const float* po, const float2* pml, 
   for (int k = 0; k < kCombineDepth; ++k) {
     const float mk = __shfl_sync(0xffffffffu, ml.x, k, 16);
     const float lk = __shfl_sync(0xffffffffu, ml.y, k, 16);
-    if (lk > 0.f) {  // also false past the group's last split
+    if (lk != 0.f) {  // also false past the group's last split
       const float w = ex2(mk - m_g);
       l_g = fmaf(w, lk, l_g);
       fma4(acc, w, v[k]);
@@ -589,7 +591,7 @@ __device__ __forceinline__ void merge_group(const float* po, const float2* pml, 
   if (active) {
     for (int s = sub + gpr * kCombineDepth; s < nsplit; s += gpr) {
       const float2 x = pml[(int64_t)s * ml_stride];
-      if (x.y > 0.f) {
+      if (x.y != 0.f) {
         if (x.x > m_g) {
           const float c = m_g == -INFINITY ? 0.f : ex2(m_g - x.x);
           l_g *= c;
@@ -698,13 +700,13 @@ __global__ void __cluster_dims__(kSlices, 1, 1) __launch_bounds__(kCombineThread
     for (int g = 0; g < gpr; ++g) M = fmaxf(M, grp_m[g0 + g]);
     float L = 0.f, t = 0.f;
     for (int g = 0; g < gpr; ++g) {
-      if (grp_l[g0 + g] > 0.f) {
+      if (grp_l[g0 + g] != 0.f) {
         const float w = ex2(grp_m[g0 + g] - M);
         L = fmaf(w, grp_l[g0 + g], L);
         t = fmaf(w, reinterpret_cast<const float*>(&acc_s[g0 + g][0])[d], t);
       }
     }
-    o_s[rr][d] = L > 0.f ? t / L : 0.f;
+    o_s[rr][d] = L == 0.f ? 0.f : t / L;
   }
   __syncthreads();
 
@@ -826,10 +828,10 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int g0 = rr * gpr;
     float M = -INFINITY;
     for (int g = 0; g < gpr; ++g)
-      if (grp_l[g0 + g] > 0.f) M = fmaxf(M, grp_m[g0 + g]);
+      if (grp_l[g0 + g] != 0.f) M = fmaxf(M, grp_m[g0 + g]);
     float L = 0.f, t = 0.f;
     for (int g = 0; g < gpr; ++g) {
-      if (grp_l[g0 + g] > 0.f) {
+      if (grp_l[g0 + g] != 0.f) {
         const float w = ex2(grp_m[g0 + g] - M);
         L = fmaf(w, grp_l[g0 + g], L);
         t = fmaf(w, reinterpret_cast<const float*>(&acc_s[g0 + g][0])[d], t);
@@ -903,17 +905,17 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int g0 = rr * gpr;
     float M = -INFINITY;
     for (int g = 0; g < gpr; ++g)
-      if (grp_l[g0 + g] > 0.f) M = fmaxf(M, grp_m[g0 + g]);
+      if (grp_l[g0 + g] != 0.f) M = fmaxf(M, grp_m[g0 + g]);
     float L = 0.f, t0 = 0.f, t1 = 0.f;
     for (int g = 0; g < gpr; ++g) {
-      if (grp_l[g0 + g] > 0.f) {
+      if (grp_l[g0 + g] != 0.f) {
         const float w = ex2(grp_m[g0 + g] - M);
         L = fmaf(w, grp_l[g0 + g], L);
         t0 = fmaf(w, reinterpret_cast<const float*>(&acc_s[g0 + g][0])[d], t0);
         t1 = fmaf(w, reinterpret_cast<const float*>(&acc_s[g0 + g][0])[d + 1], t1);
       }
     }
-    const float a = L > 0.f ? t0 / L : 0.f, c = L > 0.f ? t1 / L : 0.f;
+    const float a = L == 0.f ? 0.f : t0 / L, c = L == 0.f ? 0.f : t1 / L;
     const __nv_bfloat162 hv = __floats2bfloat162_rn(a, c);
     const __nv_bfloat162 lv = __floats2bfloat162_rn(a - __low2float(hv), c - __high2float(hv));
     const int64_t off = ((int64_t)(r0 + rr) * kHeads + h) * kDLatent + slice * kSliceDims + d;
