@@ -6,6 +6,7 @@ import torch
 
 from mla_latent_kv_yarn_b200 import seq_parallel as sp
 from mla_latent_kv_yarn_b200 import session, xmla
+from oracle import mla_oracle as om
 import shared_cases as sc
 from gpu_cases import cfgs
 
@@ -21,6 +22,12 @@ def copies_prefix(batch, q_len, pages, longest):
     f, n = xmla.xmla_decode_shared_workspace_size, session.num_sms()
     more = f(batch, q_len, pages + 4096, longest + 4096 * PAGE, n) - f(batch, q_len, pages, longest, n)
     return more >= 4096 * PAGE * ROW_BYTES
+
+
+def copies_own(batch, q_len, pages, longest):
+    """Whether the own parts (of more than 256 + q_len tokens of room) are copied too."""
+    f, n = xmla.xmla_decode_shared_workspace_size, session.num_sms()
+    return f(batch, q_len, pages, longest, n) - f(batch, q_len, pages, longest - 256, n) >= batch * 256 * ROW_BYTES
 
 
 def run(st, prefix, q, longest, cfg, dec=None):
@@ -96,3 +103,167 @@ def test_a_nan_row_reaches_the_output_of_a_sharded_decode():
     torch.cuda.synchronize()
     assert torch.isnan(out[0]).all()
     sc.assert_decode_close(out[1:], sc.shared_reference(st, prefix, q, ocfg)[1:])
+
+
+# ---------------------------------------------------------------- scores that rise late
+
+# Every 256 tokens hold one token of each size in turn: a row's maximum rises by far
+# more than its lazy border of 8 (log2 units) in the second and third block of three,
+# wherever a run's segment begins.
+SIZES = (2.0, 8.0, 30.0)
+
+
+def rising_state(batch, q_len, pages, own, seed):
+    st, prefix, q, longest = sc.shared_state(batch, q_len, pages, own, seed=seed, scale=0.3)
+    for k in range(pages * PAGE // 256):
+        t = 256 * k + (37 * k + 11) % 256
+        st.pool[prefix[t // PAGE].long(), t % PAGE] *= SIZES[k % 3]
+    for b, n in enumerate(own):
+        for k in range((n - q_len + 1) // 256):
+            t = 256 * k + (53 * k + 29) % 256
+            st.pool[st.block_table[b, pages + t // PAGE].long(), t % PAGE] *= SIZES[k % 3]
+    return st, prefix, q, longest
+
+
+def bound_and_reference(st, prefix, q, ocfg, few):
+    """(|out - reference| at most, reference, whether each row's maximum rises late).
+
+    As in shared_cases.shared_error_bound, with what these states add:
+    E: scores off by 2^-11 (fp16 query; with few queries hi + lo parts, 2^-16) and
+       2^-14 (float32 sums) of their sum of magnitudes change the output by at most
+       (e^(2E) - 1) sum p |v - o|.
+    Probabilities rounded to fp16: 2^-11 sum p |v| and, below 2^-14, half a step of
+       2^-24: 2^-25 against a sum of at least 2^7 (the reference maximum's own), 2^-32
+       max |v| per token.  Rounded to bf16 (few queries: all tokens, summed as rounded):
+       2^-8 sum p |v - o|.
+    Accumulation in float32 over a segment of at most 10 blocks, 160 steps of 2^-23
+       each: under 2^-15 sum p |v|.
+    Merged rows as two bf16 parts: 2^-16 sum_c |x_c W_UV[c]|; output rounded to bf16:
+       2^-8 of the value and of the errors before it."""
+    B, J = q.shape[:2]
+    n0 = prefix.numel() * PAGE
+    scale = om.softmax_scale(ocfg)
+    wk, wv = st.W_UK.double(), st.W_UV.double()
+    ref = torch.zeros(B, J, sc.H, sc.V, dtype=torch.float64, device=q.device)
+    bound = torch.zeros_like(ref)
+    late = torch.zeros(B, J, sc.H, dtype=torch.bool, device=q.device)
+    head = st.pool[prefix.long()].reshape(n0, sc.ROW).double()
+    for b in range(B):
+        n = int(st.seqlens[b])
+        rows = torch.cat([head, st.pool[sc.own_table(st, b, prefix, n)].reshape(-1, sc.ROW)[:n - n0].double()])
+        pos = torch.arange(n - J, n, device=q.device)
+        hidden = torch.arange(n, device=q.device)[None] > pos[:, None]
+        for h in range(sc.H):
+            x = q[b, :, h].double()
+            x = torch.cat([x[:, :sc.NOPE] @ wk[h], sc.rotated(x[:, sc.NOPE:], pos, ocfg)], -1) * scale
+            s = (x @ rows.T).masked_fill(hidden, -torch.inf)
+            top = s[:, :n0 // 256 * 256].reshape(J, -1, 256).amax(-1) / torch.log(torch.tensor(2.0))
+            late[b, :, h] = (top[:, 1:] > top[:, :-1] + 10).any(-1)
+            p = torch.softmax(s, -1)
+            v = rows[:, :sc.LATENT] @ wv[h]
+            o = p @ v
+            ref[b, :, h] = o
+            E = ((2.0 ** -16 if few else 2.0 ** -11) + 2.0 ** -14) * (x.abs() @ rows.abs().T).amax(-1)
+            parts = 2.0 ** -16 * ((p @ rows[:, :sc.LATENT]).abs() @ wv[h].abs())
+            pv = p @ v.abs()
+            for j in range(J):
+                away = (p[j, :, None] * (v - o[j]).abs()).sum(0)
+                e = torch.expm1(2 * E[j]) * away + 2.0 ** -15 * pv[j] + parts[j]
+                if few:
+                    e = e + 2.0 ** -8 * away
+                else:
+                    e = e + 2.0 ** -11 * pv[j] + n * 2.0 ** -32 * v.abs().amax(0)
+                bound[b, j, h] = e + 2.0 ** -8 * (o[j].abs() + e) + 1e-6
+    return bound, ref, late
+
+
+@pytest.mark.parametrize("batch,q_len,pages,own,shares", [
+    (4, 1, 192, [3, 300, 64, 700], False),
+    (6, 1, 640, [3, 1200, 64, 700, 1, 1279], True),
+    (3, 2, 640, [2, 1200, 700], True),
+    (40, 1, 256, [1 + 19 * b for b in range(40)], True),
+    (5, 8, 192, [8, 1200, 700, 300, 999], True)])
+def test_scores_that_rise_late(batch, q_len, pages, own, shares):
+    cfg, ocfg = cfgs()
+    st, prefix, q, longest = rising_state(batch, q_len, pages, own, seed=30 + batch)
+    assert copies_prefix(batch, q_len, pages, longest) == shares
+    if shares:
+        assert copies_own(batch, q_len, pages, longest)
+        # every run holds four blocks and more: one of each size behind its first
+        tiles = -(-batch * q_len * sc.H // 128)
+        assert tiles * (pages // 4 + 1) >= 4 * (session.num_sms() // 2)
+    out, dec = run(st, prefix, q, longest, cfg)
+    assert dec.check_status() == 0
+    bound, ref, late = bound_and_reference(st, prefix, q, ocfg, few=not shares)
+    assert float(late.double().mean()) > 0.9
+    over = float(((out.double() - ref).abs() - bound).max())
+    assert over <= 0.0, over
+    # the bound says something: a result without the rescale would be off by the
+    # size of the output
+    assert float(bound.norm() / ref.norm()) < 0.5
+
+
+# ---------------------------------------------------------------- bad block ids
+
+SHARES = [(3, 1, False), (6, 1, True), (3, 4, True), (40, 1, True)]
+
+
+@pytest.mark.parametrize("batch,q_len,shares", SHARES)
+def test_bad_prefix_block(batch, q_len, shares):
+    cfg, ocfg = cfgs()
+    st, prefix, q, longest = sc.shared_state(batch, q_len, 6, [q_len + (13 * b) % 90 for b in range(batch)], seed=40)
+    assert copies_prefix(batch, q_len, 6, longest) == shares
+    zeroed = session.LayerState(**{**st.__dict__, "pool": st.pool.clone()})
+    zeroed.pool[prefix[4].long()] = 0
+    ref = sc.shared_reference(zeroed, prefix, q, ocfg)
+    for bad in (-1, st.num_blocks, 2 ** 31 - 1, -2 ** 31):
+        broken = prefix.clone()
+        broken[4] = bad
+        out, dec = run(st, broken, q, longest, cfg)
+        assert dec.check_status() == 5
+        sc.assert_decode_close(out, ref, f"block {bad}")
+
+
+@pytest.mark.parametrize("room", [400, 100000])
+@pytest.mark.parametrize("batch,q_len,shares", SHARES)
+def test_bad_own_block(batch, q_len, shares, room):
+    cfg, ocfg = cfgs()
+    own = [q_len + (13 * b) % 90 for b in range(batch)]
+    own[1] = 350
+    st, prefix, q, longest = sc.shared_state(batch, q_len, 6, own, seed=41, room=room)
+    assert copies_prefix(batch, q_len, 6, longest) == shares
+    assert copies_own(batch, q_len, 6, longest) == (shares and room == 400)
+    zeroed = session.LayerState(**{**st.__dict__, "pool": st.pool.clone()})
+    zeroed.pool[st.block_table[1, 8].long()] = 0
+    ref = sc.shared_reference(zeroed, prefix, q, ocfg)
+    for bad in (-1, st.num_blocks, 2 ** 31 - 1, -2 ** 31):
+        table = st.block_table.clone()
+        table[1, 8] = bad
+        out, dec = run(session.LayerState(**{**st.__dict__, "block_table": table}), prefix, q, longest, cfg)
+        assert dec.check_status() == 5
+        sc.assert_decode_close(out, ref, f"block {bad}")
+
+
+# ---------------------------------------------------------------- one buffer, several plans
+
+def test_one_workspace_for_calls_of_different_sizes():
+    """A large batch, a smaller one, few queries and the large one again in the same
+    buffer: each finds the tables and partials of the call before it."""
+    cfg, ocfg = cfgs()
+    sizes = [(130, 1, 5, [1 + 2 * b for b in range(130)], 0), (6, 2, 9, [2, 70, 300, 64, 5, 2], 0),
+             (2, 1, 9, [2, 500], 0), (6, 1, 3, [1, 2, 3, 4, 5, 6], 60000),
+             (1, 1, 1, [1], 0), (130, 1, 5, [261 - 2 * b for b in range(130)], 0)]
+    states = [sc.shared_state(b, j, pages, own, seed=50 + i, room=room)
+              for i, (b, j, pages, own, room) in enumerate(sizes)]
+    decs = [session.SharedDecoder(q.shape[0], q.shape[1], prefix.numel(), longest, "cuda")
+            for st, prefix, q, longest in states]
+    buffer = torch.full((max(d.ws_bytes for d in decs),), 0xFF, dtype=torch.uint8, device="cuda")
+    for d in decs:
+        d.workspace = buffer
+    scale = xmla.xmla_softmax_scale(cfg, 192)
+    for d, (st, prefix, q, longest) in zip(decs, states):  # one right behind the other
+        d.decode(cfg, st, prefix, q, scale)
+    torch.cuda.synchronize()
+    for i, (d, (st, prefix, q, longest)) in enumerate(zip(decs, states)):
+        assert d.check_status() == 0
+        sc.assert_decode_close(d.out, sc.shared_reference(st, prefix, q, ocfg), f"call {i}")
