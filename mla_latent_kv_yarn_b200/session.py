@@ -237,6 +237,24 @@ def _on(stream):
                              else torch.cuda.ExternalStream(int(stream)))
 
 
+class _Column:
+    """The address of t's column c, for a library call (a slice of t costs the host 2 us,
+    a quarter of the smallest append)."""
+
+    def __init__(self, t: torch.Tensor, c: int):
+        self.address = t.data_ptr() + c * t.element_size()
+
+    def data_ptr(self) -> int:
+        return self.address
+
+
+def _row(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> None:
+    """t holds at least n values of dtype, one behind the other."""
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} values of {dtype}, one behind the other: "
+                         f"it is {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
 def norm_rope_rows(cfg, x: torch.Tensor, weight: torch.Tensor | None, eps: float,
                    positions: torch.Tensor | None = None, out=None, stream=None) -> torch.Tensor:
     """Norm of every head of x [R, H, D] (weight [D] or [H, D]) and, with a cfg, the
@@ -245,12 +263,28 @@ def norm_rope_rows(cfg, x: torch.Tensor, weight: torch.Tensor | None, eps: float
     if out is None:
         with _on(stream):
             out = torch.empty((R, H, D), dtype=x.dtype, device=x.device)
-    for t in (x, out, weight):
-        if t is not None and D > 1 and t.stride(-1) != 1:
-            raise ValueError("a head's values must be adjacent")
-    wh = weight.stride(0) if weight is not None and weight.dim() == 2 else 0
-    xmla.xmla_norm_rope(cfg, x, x.stride(0), x.stride(1), out, out.stride(0), out.stride(1), R, H, D,
-                        weight, wh, eps, D - D_ROPE if cfg is not None else 0, positions, stream)
+    elif out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError(f"out is {out.dtype} {tuple(out.shape)}, x {x.dtype} {tuple(x.shape)}")
+    if x.dtype is not torch.bfloat16:
+        raise ValueError(f"x is {x.dtype}, not bfloat16")
+    x_row, x_head, x_in = x.stride()
+    o_row, o_head, o_in = out.stride()
+    if D > 1 and (x_in != 1 or o_in != 1):
+        raise ValueError("a head's values must be adjacent")
+    wh = 0
+    if weight is not None:
+        if weight.dim() == 2:
+            wh = weight.stride(0)
+            if weight.shape != (H, D) or weight.dtype is not x.dtype or (D > 1 and weight.stride(1) != 1):
+                raise ValueError("a weight of each head must be bfloat16 [H, D], its values adjacent")
+        elif weight.dim() != 1 or weight.shape[0] != D:
+            raise ValueError(f"weight is {tuple(weight.shape)}, neither ({D},) nor ({H}, {D})")
+        else:
+            _row(weight, torch.bfloat16, D, "weight")
+    if cfg is not None and positions is not None:
+        _row(positions, torch.int64, R, "positions")
+    xmla.xmla_norm_rope(cfg, x, x_row, x_head, out, o_row, o_head, R, H, D, weight, wh, eps,
+                        D - D_ROPE if cfg is not None else 0, positions, stream)
     return out
 
 
@@ -258,11 +292,23 @@ def append_normed_rows(cfg, st: LayerState, kv: torch.Tensor, kv_weight: torch.T
                        pe_weight: torch.Tensor | None, eps: float, positions: torch.Tensor,
                        seq_ids: torch.Tensor, status=None, stream=None) -> None:
     """Norm, rotate and append the rows of a raw key projection kv [T, 576] =
-    [c_kv | k_pe] to st's cache (bf16 or 8-bit)."""
+    [c_kv | k_pe] (rows at any multiple of 8 values, a row's values adjacent) to st's
+    cache (bf16 or 8-bit)."""
+    T, width = kv.shape
+    stride, inner = kv.stride()
+    if width < D_LATENT + D_ROPE or inner != 1 or kv.dtype is not torch.bfloat16:
+        raise ValueError("kv must be bfloat16 [T, 576] with a row's values adjacent")
+    _row(kv_weight, torch.bfloat16, D_LATENT, "kv_weight")
+    if pe_weight is not None:
+        _row(pe_weight, torch.bfloat16, D_ROPE, "pe_weight")
+    _row(positions, torch.int64, T, "positions")
+    _row(seq_ids, torch.int32, T, "seq_ids")
+    if T == 1:
+        stride = D_LATENT + D_ROPE  # (torch gives a single row any stride)
     append = xmla.xmla_cache_append_norm_q8 if st.cache == "q8" else xmla.xmla_cache_append_norm
     append(st.pool, st.num_blocks, st.block_table, st.max_blocks, st.block_table.shape[0], seq_ids,
-           positions, kv, kv.stride(0), kv[:, D_LATENT:], kv.stride(0), kv_weight, pe_weight, eps,
-           cfg, kv.shape[0], status, stream)
+           positions, kv, stride, _Column(kv, D_LATENT), stride, kv_weight, pe_weight, eps, cfg, T,
+           status, stream)
 
 
 def read_back_q8(st: LayerState, seqlens: list[int], status=None, stream=None) -> LayerState:

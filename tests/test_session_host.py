@@ -50,3 +50,90 @@ def test_shared_decode_refuses_an_8bit_cache():
 def test_read_back_refuses_a_bf16_cache():
     with pytest.raises(ValueError, match="8-bit cache"):
         session.read_back_q8(state("bf16"), [70, 70])
+
+
+def refused(f, match):
+    with pytest.raises(ValueError, match=match):
+        f()
+
+
+def reaches(f):
+    with pytest.raises(AssertionError, match="reached the library"):
+        f()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "q8"])
+def test_append_normed_rows_refuses_what_it_would_misread(cache):
+    st, T, bf = state(cache), 3, torch.bfloat16
+    good = dict(kv=torch.zeros(T, 576, dtype=bf), kv_weight=torch.ones(512, dtype=bf),
+                pe_weight=torch.ones(64, dtype=bf), positions=torch.zeros(T, dtype=torch.int64),
+                seq_ids=torch.zeros(T, dtype=torch.int32))
+
+    def call(**over):
+        a = {**good, **over}
+        session.append_normed_rows(None, st, a["kv"], a["kv_weight"], a["pe_weight"], 1e-6, a["positions"],
+                                   a["seq_ids"])
+
+    reaches(call)
+    reaches(lambda: call(pe_weight=None))
+    reaches(lambda: call(kv=torch.zeros(T, 640, dtype=bf)[:, :576]))
+    reaches(lambda: call(kv=torch.zeros(T, 640, dtype=bf)[:, 64:]))
+    reaches(lambda: call(positions=torch.zeros(T + 1, dtype=torch.int64)))
+    refused(lambda: call(kv=torch.zeros(T, 1152, dtype=bf)[..., ::2]), "adjacent")
+    refused(lambda: call(kv=torch.zeros(576, T, dtype=bf).t()), "adjacent")
+    refused(lambda: call(kv=torch.zeros(T, 512, dtype=bf)), "576")
+    refused(lambda: call(kv=torch.zeros(T, 576)), "kv must")
+    refused(lambda: call(kv_weight=torch.ones(1024, dtype=bf)[::2]), "kv_weight")
+    refused(lambda: call(kv_weight=torch.ones(511, dtype=bf)), "kv_weight")
+    refused(lambda: call(kv_weight=torch.ones(512)), "kv_weight")
+    refused(lambda: call(pe_weight=torch.ones(128, dtype=bf)[::2]), "pe_weight")
+    refused(lambda: call(pe_weight=torch.ones(32, dtype=bf)), "pe_weight")
+    refused(lambda: call(positions=torch.zeros(T, dtype=torch.int32)), "positions")
+    refused(lambda: call(positions=torch.zeros(T - 1, dtype=torch.int64)), "positions")
+    refused(lambda: call(positions=torch.zeros(2 * T, dtype=torch.int64)[::2]), "positions")
+    refused(lambda: call(seq_ids=torch.zeros(T, dtype=torch.int64)), "seq_ids")
+    refused(lambda: call(seq_ids=torch.zeros(T - 1, dtype=torch.int32)), "seq_ids")
+
+
+def test_a_single_row_of_any_stride_is_appended(monkeypatch):
+    """torch gives a dimension of one any stride; the library wants a row's pitch."""
+    seen = {}
+    monkeypatch.setattr(xmla, "xmla_cache_append_norm",
+                        lambda *a: seen.update(c_stride=a[8], k_stride=a[10], T=a[15]))
+    kv = torch.zeros(576, 1, dtype=torch.bfloat16).t()
+    assert kv.shape == (1, 576) and kv.stride(0) == 1
+    session.append_normed_rows(None, state(), kv, torch.ones(512, dtype=torch.bfloat16), None, 1e-6,
+                               torch.zeros(1, dtype=torch.int64), torch.zeros(1, dtype=torch.int32))
+    assert seen == dict(c_stride=576, k_stride=576, T=1)
+
+
+def test_norm_rope_rows_refuses_what_it_would_misread():
+    R, H, D, bf = 3, 4, 192, torch.bfloat16
+    cfg = object()  # (a call that is not refused ends before it is looked at)
+    good = dict(x=torch.zeros(R, H, D, dtype=bf), weight=torch.ones(D, dtype=bf),
+                positions=torch.zeros(R, dtype=torch.int64), out=None)
+
+    def call(cfg=cfg, **over):
+        a = {**good, **over}
+        session.norm_rope_rows(cfg, a["x"], a["weight"], 1e-6, a["positions"], a["out"])
+
+    reaches(call)
+    reaches(lambda: call(weight=None))
+    reaches(lambda: call(weight=torch.ones(H, D, dtype=bf)))
+    reaches(lambda: call(weight=torch.ones(D, dtype=bf).expand(H, D)))
+    reaches(lambda: call(cfg=None, positions=None))
+    reaches(lambda: call(x=torch.zeros(H, R, D, dtype=bf).transpose(0, 1)))
+    reaches(lambda: call(out=torch.zeros(R, 2 * H, D, dtype=bf)[:, ::2]))
+    refused(lambda: call(x=torch.zeros(R, H, 2 * D, dtype=bf)[..., ::2]), "adjacent")
+    refused(lambda: call(x=torch.zeros(R, H, D)), "x is")
+    refused(lambda: call(weight=torch.ones(2 * D, dtype=bf)[::2]), "one behind")
+    refused(lambda: call(weight=torch.ones(H, 2 * D, dtype=bf)[:, ::2]), "adjacent")
+    refused(lambda: call(weight=torch.ones(H, D)), "weight")
+    refused(lambda: call(weight=torch.ones(1, D, dtype=bf)), "weight")
+    refused(lambda: call(weight=torch.ones(D - 1, dtype=bf)), "weight")
+    refused(lambda: call(weight=torch.ones(D)), "weight")
+    refused(lambda: call(out=torch.zeros(R - 1, H, D, dtype=bf)), "out")
+    refused(lambda: call(out=torch.zeros(R, H, D)), "out")
+    refused(lambda: call(positions=torch.zeros(R, dtype=torch.int32)), "positions")
+    refused(lambda: call(positions=torch.zeros(R - 1, dtype=torch.int64)), "positions")
+    refused(lambda: call(positions=torch.zeros(2 * R, dtype=torch.int64)[::2]), "positions")
