@@ -218,7 +218,15 @@ class SharedDecoder:
         read as bf16 rows it would end outside the pool)."""
         if st.cache != "bf16":
             raise ValueError("the shared-prefix decode reads a bf16 cache (read_back_q8 makes one)")
-        out = self.out if out is None else out
+        units = self.batch * self.q_len
+        _row(prefix_table, torch.int32, self.prefix_pages, "prefix_table")
+        _row(q, torch.bfloat16, units * N_HEADS * (D_NOPE + D_ROPE), "q")
+        if st.seqlens.numel() < self.batch or st.block_table.numel() < self.batch * st.max_blocks:
+            raise ValueError(f"the state has fewer than {self.batch} sequences")
+        if out is None:
+            out = self.out
+        else:
+            _row(out, torch.bfloat16, units * N_HEADS * D_V, "out")
         xmla.xmla_decode_shared(cfg, q, st.W_UK, st.W_UV, st.pool, st.num_blocks, prefix_table,
                                 self.prefix_pages, st.block_table, st.max_blocks, st.seqlens,
                                 self.batch, self.q_len, self.max_seqlen, softmax_scale,

@@ -137,3 +137,28 @@ def test_norm_rope_rows_refuses_what_it_would_misread():
     refused(lambda: call(positions=torch.zeros(R, dtype=torch.int32)), "positions")
     refused(lambda: call(positions=torch.zeros(R - 1, dtype=torch.int64)), "positions")
     refused(lambda: call(positions=torch.zeros(2 * R, dtype=torch.int64)[::2]), "positions")
+
+
+def test_shared_decode_refuses_less_than_its_sizes():
+    """A decoder made for more sequences, queries or prefix pages than the call brings
+    would read behind the tensors (and write behind out)."""
+    bf = torch.bfloat16
+    good = dict(st=state(), prefix=torch.zeros(1, dtype=torch.int32), q=torch.zeros(2, 1, 32, 192, dtype=bf), out=None)
+
+    def call(dec=None, **over):
+        a = {**good, **over}
+        (dec or shared_decoder()).decode(None, a["st"], a["prefix"], a["q"], 0.1, a["out"])
+
+    reaches(call)
+    reaches(lambda: call(prefix=torch.zeros(3, dtype=torch.int32)))
+    reaches(lambda: call(out=torch.zeros(2, 1, 32, 128, dtype=bf)))
+    refused(lambda: call(prefix=torch.zeros(0, dtype=torch.int32)), "prefix_table")
+    refused(lambda: call(prefix=torch.zeros(1, dtype=torch.int64)), "prefix_table")
+    refused(lambda: call(shared_decoder(prefix_pages=2)), "prefix_table")
+    refused(lambda: call(prefix=torch.zeros(4, dtype=torch.int32)[::2], dec=shared_decoder(prefix_pages=2)), "prefix")
+    refused(lambda: call(q=torch.zeros(1, 1, 32, 192, dtype=bf)), "q must")
+    refused(lambda: call(q=torch.zeros(2, 1, 32, 192)), "q must")
+    refused(lambda: call(q=torch.zeros(2, 1, 192, 32, dtype=bf).transpose(2, 3)), "q must")
+    refused(lambda: call(shared_decoder(q_len=2)), "q must")
+    refused(lambda: call(out=torch.zeros(1, 1, 32, 128, dtype=bf)), "out must")
+    refused(lambda: call(st=state(batch=1)), "sequences")
