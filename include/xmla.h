@@ -136,7 +136,8 @@ xmla_status xmla_cache_append(void* pool, int64_t num_blocks, const int32_t* blo
  * and, when cfg is not NULL, the 64 values from rope_offset on are then rotated
  * at positions[r] as xmla_rope_yarn pairs them (i with i + 32).  The norm and
  * the rotation run in float32 (the angle is formed in float64 from the exact
- * position); the result is rounded to bf16 once.
+ * position; a vector whose squares would leave float32's range is scaled by a
+ * power of two first); the result is rounded to bf16 once.
  *   cfg: YaRN parameters, or NULL: no rotation (rope_offset and positions are
  *      ignored).  xmla_decode rotates its query itself: give it one normed
  *      with cfg NULL;
@@ -166,7 +167,7 @@ xmla_status xmla_norm_rope(const xmla_yarn_cfg* cfg, const void* x, int64_t x_ro
  *   k = k_pe                                          if pe_weight is NULL
  *   k = k_pe / sqrt(mean(k_pe^2) + eps) * pe_weight   otherwise
  * with the rotation left out when rope_cfg is NULL; float32 throughout (angles
- * from float64), rounded to bf16 once.
+ * from float64; norms at any magnitude, as in xmla_norm_rope), rounded to bf16 once.
  *   c_kv: device bf16, row i at i*c_stride (elements, >= 512, a multiple of 8;
  *      16-byte aligned); k_pe: device bf16, row i at i*k_stride (>= 64).  Both
  *      may be columns of one [T, 576] projection (c_stride = k_stride = 576);

@@ -109,31 +109,45 @@ __global__ void __launch_bounds__(32 * kAnWarps, 4)
   }
   // (the values stay packed between the passes over them: unpacked, they would
   // take the registers of a block per SM)
-  float sq = 0.f, sq_pe = 0.f;
+  float sq, sq_pe;
+  auto squares = [&](float scale) {
+    sq = sq_pe = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float x[8];
-    unpack8(xv[k], x);
+    for (int k = 0; k < 4; ++k) {
+      float x[8];
+      unpack8(xv[k], x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-    sq_pe = fmaf(y[k], y[k], sq_pe);
+      for (int e = 0; e < 8; ++e) sq = fmaf(x[e] * scale, x[e] * scale, sq);
+      sq_pe = fmaf(y[k], y[k], sq_pe);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      sq_pe += __shfl_xor_sync(0xffffffffu, sq_pe, o);
+    }
+  };
+  squares(1.f);
+  float eps = a.eps, eps_pe = a.eps;
+  const float scale = rms_scale(sq, kDLatent, eps);
+  const float scale_pe = a.w_pe != nullptr ? rms_scale(sq_pe, kDRope, eps) : 1.f;
+  if (__any_sync(0xffffffffu, scale != 1.f || scale_pe != 1.f)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] *= scale_pe;
+    squares(scale);
+    eps = eps * scale * scale;
+    eps_pe = eps_pe * scale_pe * scale_pe;
   }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    sq_pe += __shfl_xor_sync(0xffffffffu, sq_pe, o);
-  }
-  const float f = rms_factor(sq, kDLatent, a.eps);
+  const float f = rms_factor(sq, kDLatent, eps);
   // piece k of the normed latent; the weights come from L1
   auto latent = [&](int k, float (&x)[8]) {
     float w[8];
     unpack8(xv[k], x);
     unpack8(*reinterpret_cast<const uint4*>(a.w_kv + 8 * (l + 16 * k)), w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= f * w[e];
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * (f * w[e]);
   };
   if (a.w_pe != nullptr) {
-    const float g = rms_factor(sq_pe, kDRope, a.eps);
+    const float g = rms_factor(sq_pe, kDRope, eps_pe);
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] *= g * __bfloat162float(a.w_pe[l + 16 * k]);
   }

@@ -52,4 +52,17 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// What a vector's values are to be multiplied by before they are squared, given the
+// float32 sum sq of their plain squares: 1, unless that sum overflowed (|x| from
+// 2^59 on) or mean and eps together are so small that squares were lost below the
+// normal range.  bf16 values times 2^-70 are below 2^58, and 1024 squares of them
+// below 2^126; values that take 2^90 (under 2^-45 for 1024 of them) stay below 2^45,
+// and the smallest bf16 value becomes 2^-43.  The norm is then (x S) * (f w) with f =
+// rms_factor(sum of (x S)^2, n, eps S S): the power of two cancels, and S = 1, the
+// usual case, changes nothing.
+__device__ __forceinline__ float rms_scale(float sq, int n, float eps) {
+  const float v = sq / (float)n + eps;
+  return v < 0x1p-100f ? 0x1p90f : v < INFINITY ? 1.f : 0x1p-70f;
+}
+
 }  // namespace xmla
