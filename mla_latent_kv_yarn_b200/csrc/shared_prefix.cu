@@ -1363,7 +1363,10 @@ __global__ void __cluster_dims__(kOutSplit, 1, 1) __launch_bounds__(kOutThreads)
     *reinterpret_cast<uint4*>(out + ((int64_t)(r0 + rr) * kHeads + h) * kDV + 32 * k + 8 * u) =
         pack8(x);
   }
-  if (warp == 1) tmem_dealloc(tmem, 128);
+  if (warp == 1) {
+    __syncwarp();  // its lanes leave the loop after different numbers of rounds
+    tmem_dealloc(tmem, 128);
+  }
 }
 
 cudaError_t launch_shared_out(const CUtensorMap& hi_map, const CUtensorMap& lo_map,

@@ -267,3 +267,17 @@ def test_one_workspace_for_calls_of_different_sizes():
     for i, (d, (st, prefix, q, longest)) in enumerate(zip(decs, states)):
         assert d.check_status() == 0
         sc.assert_decode_close(d.out, sc.shared_reference(st, prefix, q, ocfg), f"call {i}")
+
+
+@pytest.mark.parametrize("batch", [5, 6, 7, 8, 9, 11, 13, 15, 16, 17, 31, 33, 47, 48, 49, 127, 128, 129, 137])
+def test_every_remainder_of_output_rows(batch):
+    """Numbers of queries that leave the W_UV kernel's warps at different rows, and its
+    boxes of eight rows partly filled; nothing behind the last row is written."""
+    cfg, ocfg = cfgs()
+    st, prefix, q, longest = sc.shared_state(batch, 1, 2, [1 + (5 * b) % 70 for b in range(batch)], seed=70 + batch)
+    dec = session.SharedDecoder(batch, 1, 2, longest, "cuda")
+    out = torch.full((batch + 2, 1, 32, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    dec.decode(cfg, st, prefix, q, xmla.xmla_softmax_scale(cfg, 192), out=out)
+    torch.cuda.synchronize()
+    assert dec.check_status() == 0 and bool((out[batch:] == 7.0).all())
+    sc.assert_decode_close(out[:batch], sc.shared_reference(st, prefix, q, ocfg))
