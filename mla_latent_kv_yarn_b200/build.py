@@ -19,7 +19,7 @@ SOURCES = ["rope_append.cu", "mla_decode.cu", "absorb_combine.cu", "xmla_api.cu"
            "head_gemm.cu", "mla_decode_q8.cu", "q8_append.cu", "prefill.cu", "shared_prefix.cu",
            "norm_rope.cu", "cache_norm.cu"]
 HEADERS = ["xmla_device.cuh", "yarn.cuh", "append.cuh", "decode_chain.h", "split_kv.h", "produce.cuh",
-           "prefill.h", "shared_prefix.h", "norm.cuh",
+           "prefill.h", "shared_prefix.h", "shared_plan.h", "norm.cuh",
            os.path.join("..", "..", "include", "xmla.h")]
 
 NVCC_FLAGS = [

@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "norm.cuh"
+#include "shared_plan.h"
 #include "shared_prefix.h"
 #include "xmla_device.cuh"
 
@@ -153,67 +154,6 @@ __device__ __forceinline__ int64_t group_unit(int64_t n, int64_t row, int u) {
   return ((int64_t)(u >> 3) * n + row) * 8 + (u & 7);
 }
 
-// Own tokens of sequence b: 0 where its length leaves its new tokens outside
-// its own pages (the merge reports it and zeroes its rows).
-__device__ __forceinline__ int own_tokens(const SharedParams& p, int b) {
-  const int64_t len = p.seqlens[b], first = (int64_t)p.prefix_pages * kPage;
-  return len >= first + p.q_len && len <= p.max_seqlen ? (int)(len - first) : 0;
-}
-__device__ __forceinline__ int own_blocks(int tokens) {
-  return (tokens + kSharedBlock - 1) / kSharedBlock;
-}
-
-// All places and runs; the own parts' share is known on the device only.
-__device__ __forceinline__ SharedWork shared_work(const SharedParams& p, int own_places) {
-  SharedWork w;
-  w.places = (int64_t)p.tiles * (p.blocks + 1) + own_places;
-  w.runs = (int32_t)min((int64_t)p.pairs, w.places);
-  return w;
-}
-
-// The segments of a run in order.
-struct Segments {
-  SharedRun at;
-  // the segment
-  bool is_own;
-  int tile;  // of the prefix or of the own parts
-  int b0;    // first block
-  int n;     // blocks
-  int seq, tokens;  // an own tile's sequence and its own tokens
-
-  __device__ __forceinline__ bool next(const SharedParams& p) {
-    for (; at.places > 0; ++at.tile, at.place = 0) {
-      is_own = at.tile >= p.tiles;
-      tile = is_own ? at.tile - p.tiles : at.tile;
-      int nb = p.blocks;
-      if (is_own) {
-        if (tile >= p.batch * p.own_tiles) return false;
-        seq = p.own_tiles == 1 ? tile : tile >> 1;
-        tokens = own_tokens(p, seq);
-        nb = own_blocks(tokens);
-        if (nb == 0) continue;  // a sequence of bad length has no places
-      }
-      if (at.place == 0) {
-        at.place = 1;
-        if (--at.places == 0) return false;
-      }
-      if (at.place > nb) continue;
-      b0 = at.place - 1;
-      n = (int)min((int64_t)(nb - b0), at.places);
-      at.place += n;
-      at.places -= n;
-      return true;
-    }
-    return false;
-  }
-  // first query row (of all rows) of the tile
-  __device__ __forceinline__ int64_t row0(const SharedParams& p) const {
-    if (!is_own) return (int64_t)tile * kSharedRows;
-    return ((int64_t)seq * p.q_len + (tile - seq * p.own_tiles) * kSharedOwnQ) * kHeads;
-  }
-};
-static_assert(kSharedMaxQLen <= 2 * kSharedOwnQ, "one or two tiles per sequence");
-
 }  // namespace
 
 // ---------------------------------------------------------------- absorbed queries
@@ -334,16 +274,12 @@ constexpr int kSharedOwnSeqs = (int)(kSharedOwnTokens / kSharedBlock);  // 128 s
 static_assert((kSharedOwnSeqs + 1 + 32) * 4 <= kAbSmem, "the sums of all sequences");
 __device__ __forceinline__ void plan_runs(const SharedParams& p, int* cum, int* sums) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  auto places = [&](int b) {
-    const int nb = own_blocks(own_tokens(p, b));
-    return nb > 0 ? (nb + 1) * p.own_tiles : 0;
-  };
   int own = 0;
   if (p.own16 != nullptr) {
     const int per = (p.batch + kAbThreads - 1) / kAbThreads;
     const int b0 = min(p.batch, t * per), b1 = min(p.batch, b0 + per);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += places(b);
+    for (int b = b0; b < b1; ++b) sum += own_places(p, b);
     int before = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -356,51 +292,19 @@ __device__ __forceinline__ void plan_runs(const SharedParams& p, int* cum, int* 
     for (int k = 0; k < warp; ++k) before += sums[k];
     for (int b = b0; b < b1; ++b) {
       cum[b] = before;
-      before += places(b);
+      before += own_places(p, b);
       if (b == p.batch - 1) cum[p.batch] = before;
     }
     __syncthreads();
     own = cum[p.batch];
   }
   const SharedWork w = shared_work(p, own);
-  for (int run = t; run < p.pairs; run += kAbThreads) {
-    SharedRun r{0, 0, 0};
-    if (run < w.runs) {
-      const int64_t x = w.begin(run), x_own = x - (int64_t)p.tiles * (p.blocks + 1);
-      r.places = w.begin(run + 1) - x;
-      if (x_own < 0) {
-        r.tile = (int)(x / (p.blocks + 1));
-        r.place = (int)(x % (p.blocks + 1));
-      } else {  // the last sequence with cum <= x_own has that place
-        int lo = 0, hi = p.batch - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (cum[mid] <= x_own) lo = mid;
-          else hi = mid - 1;
-        }
-        const int each = (cum[lo + 1] - cum[lo]) / p.own_tiles, k = (int)x_own - cum[lo];
-        r.tile = p.tiles + lo * p.own_tiles + k / each;
-        r.place = k % each;
-      }
-    }
-    p.run_tab[run] = r;
-  }
-  // the runs from that of a tile's first block to that of its last
-  auto partials = [&](int64_t first_place, int nb, int tile) {
-    const int run0 = w.run_of(first_place + 1);
-    return make_int2(run0 + tile, w.run_of(first_place + nb) - run0 + 1);
-  };
+  for (int run = t; run < p.pairs; run += kAbThreads) p.run_tab[run] = shared_run(p, w, run, cum);
   for (int tile = t; tile < p.tiles; tile += kAbThreads)
-    p.tile_tab[tile] = partials((int64_t)tile * (p.blocks + 1), p.blocks, tile);
+    p.tile_tab[tile] = shared_tile_partials(p, w, tile, cum);
   if (p.own16 != nullptr)
-    for (int tile = t; tile < p.batch * p.own_tiles; tile += kAbThreads) {
-      const int b = tile / p.own_tiles, each = (cum[b + 1] - cum[b]) / p.own_tiles;
-      p.tile_tab[p.tiles + tile] =
-          each == 0 ? make_int2(0, 0)
-                    : partials((int64_t)p.tiles * (p.blocks + 1) + cum[b] +
-                                   (int64_t)(tile - b * p.own_tiles) * each,
-                               each - 1, tile);
-    }
+    for (int tile = t; tile < p.batch * p.own_tiles; tile += kAbThreads)
+      p.tile_tab[p.tiles + tile] = shared_tile_partials(p, w, p.tiles + tile, cum);
 }
 
 __global__ void __launch_bounds__(kAbThreads)
@@ -1053,7 +957,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSharedThreads, 1)
       // (of an own tile, the rows of its queries only)
       const bool stored = !sg.is_own || (tile_row < p.own_rows &&
                                          sg.row0(p) + tile_row < (int64_t)(sg.seq + 1) * p.q_len * kHeads);
-      const int64_t slot = run + sg.tile;
+      const int64_t slot = sg.slot(run);
       const int slot_rows = sg.is_own ? p.own_rows : kSharedRows;
       if (ok) {
         // four columns at a time, the 32 rows of the warp side by side: 512 bytes
