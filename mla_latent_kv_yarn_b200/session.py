@@ -324,6 +324,9 @@ def read_back_q8(st: LayerState, seqlens: list[int], status=None, stream=None) -
     of consecutive pages, on which any xmla_decode call on `stream` runs."""
     if st.cache != "q8":
         raise ValueError("the rows of an 8-bit cache are read back; this one is bf16 already")
+    if len(seqlens) > st.block_table.shape[0] or any(not 0 <= n <= st.max_blocks * PAGE for n in seqlens):
+        # (their rows would be skipped and read as zeros)
+        raise ValueError("more sequences, or longer ones, than the cache's block table has")
     dev = st.pool.device
     pages = [(n + PAGE - 1) // PAGE for n in seqlens]
     first = [sum(pages[:b]) for b in range(len(pages))]

@@ -162,3 +162,11 @@ def test_shared_decode_refuses_less_than_its_sizes():
     refused(lambda: call(shared_decoder(q_len=2)), "q must")
     refused(lambda: call(out=torch.zeros(1, 1, 32, 128, dtype=bf)), "out must")
     refused(lambda: call(st=state(batch=1)), "sequences")
+
+
+def test_read_back_refuses_lengths_outside_the_table():
+    st = state("q8")  # two sequences of up to 256 tokens
+    reaches(lambda: session.read_back_q8(st, [256, 3]))
+    reaches(lambda: session.read_back_q8(st, [1]))
+    for bad in ([257, 3], [3, 300], [1, 2, 3], [-1, 4]):
+        refused(lambda: session.read_back_q8(st, bad), "block table")
