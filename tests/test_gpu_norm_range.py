@@ -114,3 +114,28 @@ def test_normed_append_over_the_whole_range(cache, with_pe, eps):
         assert float(((got.double() - ref).abs() - unit / 2 - SLACK * top).max()) <= 0.0
     torch.cuda.synchronize()
     assert int(status) == 0
+
+
+def test_codes_are_the_nearest_up_to_float32():
+    """|x / unit - code| is at most a half, up to the error of x: the squares' sum takes
+    32 + 4 steps of 2^-24, of which the factor has half, its own rounding and the
+    refinement's rest one each, the product one more: under 21 x 2^-24 < 2^-19."""
+    cfg, _ = cfgs()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    T = 4096
+    kv, w = sc.randn(g, T, 576, std=3.0), (1 + 0.1 * torch.randn(512, generator=g, device="cuda")).bfloat16()
+    blocks = T // 64
+    st = session.LayerState(pool=session.new_pool_q8(blocks, "cuda"),
+                            block_table=torch.randperm(blocks, generator=g, device="cuda").to(torch.int32)[None],
+                            seqlens=None, W_UK=None, W_UV=None, num_blocks=blocks, max_blocks=blocks, cache="q8")
+    pos, ids = torch.arange(T, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    session.append_normed_rows(cfg, st, kv, w, None, 1e-6, pos, ids)
+    rows = st.pool[st.block_table[0].long()].reshape(T, 608)
+    codes = rows[:, :512].view(torch.int8).double().reshape(T, 16, 32)
+    unit = torch.exp2(rows[:, 576:592].view(torch.int8).double())[..., None]
+    x = sc.normed(kv[:, :512], w, float(np.float32(1e-6))).reshape(T, 16, 32) / unit
+    assert float(((x - codes).abs() - 0.5 - x.abs() * 2.0 ** -19).max()) <= 0.0
+    # and the unit is the smallest that holds the block
+    top = x.abs().amax(-1)
+    assert float(top.max()) <= 127 * (1 + 2.0 ** -19) and float(top.min()) >= 63.5 * (1 - 2.0 ** -19)
