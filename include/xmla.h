@@ -426,7 +426,11 @@ xmla_status xmla_decode_step_from_hidden(const xmla_yarn_cfg* cfg, const void* q
  * Every sequence begins with the same prefix_pages full cache pages (a system
  * prompt, a document: 64 * prefix_pages tokens, written once) and goes on in
  * pages of its own.  A prefix that ends inside a page is shared up to its last
- * full page; the tokens after that belong to each sequence's own pages. */
+ * full page; the tokens after that belong to each sequence's own pages.
+ * Against xmla_decode over whole block tables it pays from about 16 sequences
+ * on, over 32K shared tokens from about 8 (measured); for fewer queries, and for
+ * one sequence with several, xmla_decode takes as long or up to a third
+ * less. */
 
 /* Bytes of device workspace xmla_decode_shared needs for these sizes on a
  * device with num_sms SMs: among others, with more than four queries in all, 1152
@@ -448,15 +452,17 @@ size_t xmla_decode_shared_workspace_size(int32_t batch, int32_t q_len, int32_t p
  *      xmla_norm_rope or xmla_rope_yarn);
  *   the other arguments as in xmla_decode (q, W_UK, W_UV and out in device
  *   memory).
- * A block id outside the pool is recorded and its page read as zeros.  The
- * products over the prefix (and over own parts of up to 32K tokens in all) run
- * in fp16 with fp32 accumulation: cache values and absorbed queries
+ * A block id outside the pool is recorded and its page read as zeros.  With
+ * more than four queries in all (batch * q_len) the products over the prefix (and
+ * over own parts with room for up to 32K tokens in all) run in fp16 with fp32
+ * accumulation: cache values and absorbed queries
  * (softmax_scale * log2(e) * W_UK^T q_nope) must stay below 65504 in magnitude;
  * a larger one becomes infinite.  Those below 2^-14 are held to 2^-25, so that a
  * cache of values below about 2^-16 loses accuracy.  A NaN in a token's row, or
  * an infinity in its latent, makes the outputs of the sequences that hold the
- * token NaN, and no others.  With up to four queries in all (batch * q_len) the
- * call attends each sequence whole, like xmla_decode.
+ * token NaN, and no others.  With up to four queries in all the call attends each
+ * sequence whole, like xmla_decode: cache values in bf16 as they are, the query as
+ * two bf16 parts, probabilities in bf16.  Own parts with more room are attended so too.
  * Supported: 1 <= batch, 1 <= q_len <= 8, 1 <= prefix_pages, batch * q_len *
  * 64 < 2^31, other limits as in xmla_decode.  Errors: XMLA_ERR_INVALID_ARG,
  * XMLA_ERR_SHAPE, XMLA_ERR_WORKSPACE, XMLA_ERR_CUDA, XMLA_ERR_UNSUPPORTED;

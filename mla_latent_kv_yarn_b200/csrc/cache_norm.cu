@@ -75,8 +75,8 @@ __device__ __forceinline__ uint32_t block_code(float x, int e) {
 // mean plus eps and of r * r, takes out those of the root and the quotient.  A code is
 // a rounding: the fewer values the float32 error takes past the middle of two codes the
 // better (67 million latent values: 112 so, 140 with rms_factor and the weight multiplied
-// to the factor first, none with sums and products in pairs of floats, which take 19%
-// longer).
+// to the factor first; with sums and products in pairs of floats, for 19% more time, only
+// those of blocks whose exponent turned on it).
 __device__ __forceinline__ float rms_factor_refined(float sq, int n, float eps) {
   const float mean = sq / (float)n, v = mean + eps, b = v - mean;
   const float rest = (mean - (v - b)) + (eps - b);  // v + rest = mean + eps
@@ -89,10 +89,10 @@ __device__ __forceinline__ float rms_factor_refined(float sq, int n, float eps) 
 // Sixteen lanes per token: lane l of them holds the 16-byte pieces l, l + 16, l +
 // 32 and l + 48 of the latent and the rotation pairs l and l + 16 (values l, l + 16
 // and those 32 on).  A whole warp per token has half as many values per lane for
-// the same lookups, norm factors and addresses: 15,001 tokens (35 MB) 12.8 us, and
-// 11.2 us with sixteen lanes; 16,384 tokens to the 8-bit pool and read back 24.4
-// and 21.3 us.  Bound by latency: about two waves of blocks, each a lookup, its
-// loads and its stores one after the other.
+// the same lookups, norm factors and addresses: 1.6 us more for 15,001 tokens and 3 us
+// more for 16,384 to the 8-bit pool and read back, which take 11.2 us (35 MB) and 22.3
+// us.  Bound by latency: about two waves of blocks, each a lookup, its loads and its
+// stores one after the other.
 constexpr int kAnTokens = 2 * kAnWarps;  // per block
 
 template <bool kQ8>

@@ -35,7 +35,11 @@ struct NormRopeArgs {
 // sines depend on the row alone: one warp forms them for the whole block while
 // the others fetch their heads.  kVec: 16-byte accesses (lane holds elements
 // 8 (lane + 32 k) .. + 7), else single elements lane + 32 k.  kChunks: accesses
-// per lane.
+// per lane.  Takes what the kernel below does not: heads of more than 256 values, a
+// rotated part at an offset not in multiples of 64, and odd sizes or alignments.
+// Measured on 4096 rows of 32 heads, rotated (a warp has one head in flight, and all
+// wait for the angles): 160 values with offset 96 50 us (1.7 TB/s), 512 96 us (2.8), 1024 172 us
+// (3.1), 161 one by one 82 us (1.0).
 template <bool kVec, int kChunks>
 __global__ void __launch_bounds__(32 * kNormWarps) norm_rope_kernel(const NormRopeArgs a,
                                                                     const RopeTable tab) {
@@ -175,10 +179,10 @@ __device__ __forceinline__ void norm_rope_scaled_head(const NormRopeArgs& a, int
 // multiples of 64, and piece l's rotation partner (32 values on) is piece l ^ 4 of
 // the lane four further.  Every warp forms the row's 32 cosines and sines itself,
 // one pair per lane, while its heads are on the way: no block-wide wait.
-// Measured on 4096 rows of 32 heads of 192 (101 MB): 59 us with a warp per head
-// and the angles of a block formed by one warp, 18.9 us (5.3 TB/s) with this; bound
-// by memory.
-// (five blocks per SM instead of four, where the registers allow: 20.3 -> 18.9 us)
+// Measured on 4096 rows of 32 heads of 192 (101 MB, replayed graph): 59 us with a
+// warp per head and the angles of a block formed by one warp, 19.8 us (5.1 TB/s) with
+// this; bound by memory.  Five blocks per SM instead of four, where the registers
+// allow, are worth 1.4 us of it.
 template <int kPieces>
 __global__ void __launch_bounds__(32 * kNormWarps, kPieces == 4 ? 4 : 5)
     norm_rope_group_kernel(const __grid_constant__ NormRopeArgs a, const RopeTable tab) {

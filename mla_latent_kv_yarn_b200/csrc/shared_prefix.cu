@@ -163,8 +163,8 @@ __device__ __forceinline__ int64_t group_unit(int64_t n, int64_t row, int u) {
 // of the prefix part and the hi and lo bf16 rows of the own part.  (The CUDA
 // cores took 23 us for 32 rows and 40 us for 128, re-reading W_UK for every
 // eight rows; here every CTA reads its 16 KB of it once.  Products of 128 columns
-// leave half as many CTAs with twice the row pieces to write each; us per call, 128 and
-// 64 columns: 4 sequences over 4,096 tokens 23.1 and 22.7, 32 over 32K 100.7 and 100.0,
+// leave half as many CTAs with twice the row pieces to write each; us per call in a
+// replayed graph, 128 and 64 columns: 4 sequences over 4,096 tokens 23.1 and 22.7, 32 over 32K 100.7 and 100.0,
 // 128 over 16K 188 and 177; 8 with four queries over 192 tokens 28.5 and 29.3.)
 // Blocks past the products rotate the rope parts, kRopeRowsPerBlock rows each, and
 // then plan the attention's runs and, where it has the own parts, the split-K
@@ -505,8 +505,8 @@ cudaError_t launch_shared_absorb(const CUtensorMap& q_map, const CUtensorMap& wu
 //
 // The cache rows are read once, the copies many times (by every row tile) right
 // after: the rows are loaded to be evicted first and the copies stored to be
-// evicted last (8 x 4 queries over 128K tokens, 151 MB of copies: 313..328 us per
-// call with plain accesses, 293..302 us so).
+// evicted last (8 x 4 queries over 128K tokens, 151 MB of copies, in bursts too short
+// for the power limit: 313..328 us per call with plain accesses, 293..302 us so).
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = kPage * kRowUnits / 2;  // half a page per block
 

@@ -21,19 +21,27 @@ constexpr int kSharedMaxPairs = 128;   // CTA pairs of the grid at most
 constexpr int kSharedOwnQ = 4;         // queries of a sequence in one tile of its own part
 // Own parts with room for at most this many tokens (batch * longest, rounded up to
 // blocks) are copied and attended with the prefix; larger ones go through the
-// split-K kernel, which reads them once.  Measured in us per call, together and
-// apart, over 192 shared tokens: 8 sequences with room for 1,536 tokens each 24 and
-// 35, 24 with 1,536 40 and 41, 64 with 512 and two queries 54 and 61, 64 with 1,536
-// 68 and 54, 128 with 2,048 131 and 93; over 8,192 shared tokens: 24 with 512 42 and
-// 48, 64 with 512 and two queries 108 and 103, 128 with 2,048 173 and 137.
+// split-K kernel, which reads them once.  The rule goes by room, which the host
+// knows; the lengths are on the device.  Measured in us per call (replayed graph,
+// every own part as long as its room), together and apart:
+//   over 192 shared tokens     8 sequences x 1,536  26 / 36    24 x 1,536  44 / 41
+//   over 4,096                16 x 2,048  42 / 46 (the border)
+//   over 8,192                64 x 512    74 / 73 (the border)  64 x 1,024  98 / 79
+//   over 16,448              128 x 333   168 / 147
+//   over 32,768               32 x 512    90 / 92  x 1,024  101 / 96  x 2,048  123 / 103
 constexpr int64_t kSharedOwnTokens = 1 << 15;
 
 // Up to so many queries in all, sharing does not pay for the copy: the call runs the
 // split-K kernel over each sequence's whole length, with the query as hi and lo
-// parts.  Measured in us per call, this way and by sharing, over 4,096 / 32,768 /
-// 131,072 shared tokens: one query 18 / 25 / 42 and 23 / 51 / 107; two 19 / 29 / 60
-// and 23 / 50 / 107; four 21 / 40 / 102 and 24 / 49 / 109; six 25 / 53 / 148 and
-// 25 / 52 / 129.
+// parts.  It takes as long for several queries of one sequence as for as many
+// sequences.  Measured in us per call (replayed graph, 300 own tokens), this way / by
+// sharing, over so many shared tokens:
+//   queries       64      1,024      4,096     32,768    131,072
+//      1       17 / 21    19 / 21    19 / 24    23 / 46    42 / 114
+//      2       18 / 22    20 / 22    20 / 24    28 / 47    60 / 114
+//      4       19 / 22    21 / 22    23 / 24    39 / 46   102 / 116
+//      6       21 / 23    23 / 23    26 / 26    53 / 50   149 / 139
+//      8       22 / 23    24 / 23    26 / 27    64 / 50   192 / 134
 constexpr int kSharedFewUnits = 4;
 
 // Work of the attention kernel: tiles of query rows by blocks of 256 tokens.
