@@ -152,14 +152,21 @@ __global__ void __launch_bounds__(32 * kAnWarps, 4)
     eps = eps * scale * scale;
     eps_pe = eps_pe * scale_pe * scale_pe;
   }
-  const float f = rms_factor_refined(sq, kDLatent, eps);
+  float f = rms_factor_refined(sq, kDLatent, eps);
+  // the values by the factor's power of two first (exact): their products with the
+  // weight then stay as small as the results
+  float first = scale;
+  if (scale == 1.f && f > 0x1p-126f && f < INFINITY) {
+    first = __uint_as_float(__float_as_uint(f) & 0x7f800000u);
+    f = __uint_as_float((__float_as_uint(f) & 0x007fffffu) | 0x3f800000u);
+  }
   // piece k of the normed latent; the weights come from L1
   auto latent = [&](int k, float (&x)[8]) {
     float w[8];
     unpack8(xv[k], x);
     unpack8(*reinterpret_cast<const uint4*>(a.w_kv + 8 * (l + 16 * k)), w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * w[e] * f;  // (x w is exact)
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * first * w[e] * f;  // (exact up to the last)
   };
   if (a.w_pe != nullptr) {
     const float g = rms_factor(sq_pe, kDRope, eps_pe);

@@ -139,3 +139,32 @@ def test_codes_are_the_nearest_up_to_float32():
     # and the unit is the smallest that holds the block
     top = x.abs().amax(-1)
     assert float(top.max()) <= 127 * (1 + 2.0 ** -19) and float(top.min()) >= 63.5 * (1 - 2.0 ** -19)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "q8"])
+def test_large_weights_meet_large_values(cache):
+    """x w alone would leave float32's range; the result does not."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(10)
+    T = 20
+    scale = torch.tensor([1e16, 1e-14, 1.0, 3e17, 1e-10] * 4, device="cuda")[:, None]
+    kv = (torch.randn(T, 576, generator=g, device="cuda") * scale).bfloat16()
+    w = torch.randn(512, generator=g, device="cuda").double() * (1e25 if cache == "bf16" else 1e-2)
+    w[::3] *= 1e-30 if cache == "bf16" else 1.0
+    w = w.bfloat16()
+    st = session.LayerState(pool=session.new_pool_q8(1, "cuda") if cache == "q8" else session.new_pool(1, "cuda"),
+                            block_table=torch.zeros(1, 1, dtype=torch.int32, device="cuda"), seqlens=None, W_UK=None,
+                            W_UV=None, num_blocks=1, max_blocks=1, cache=cache)
+    pos, ids = torch.arange(T, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    session.append_normed_rows(None, st, kv, w, None, 0.0, pos, ids)
+    ref = sc.normed(kv[:, :512], w, 0.0)
+    if cache == "bf16":
+        got = st.pool[0, :T, :512]
+        assert torch.isfinite(got).all()
+        over = (got.double() - ref).abs() - (HALF + SLACK) * ref.abs() - TINY
+    else:
+        got = torch.empty(T, 576, dtype=torch.bfloat16, device="cuda")
+        xmla.xmla_cache_read_q8(st.pool, 1, st.block_table, 1, 1, ids, pos, T, got, 576)
+        unit = torch.exp2(st.pool[0, :T, 576:592].view(torch.int8).double())[..., None].expand(T, 16, 32).reshape(T, 512)
+        over = (got[:, :512].double() - ref).abs() - unit / 2 - SLACK * ref.abs()
+    assert float(over.max()) <= 0.0
